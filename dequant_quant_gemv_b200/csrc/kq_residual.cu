@@ -13,15 +13,14 @@ struct ResidualArgs {
     kq_residual r;
 };
 
-__device__ __forceinline__ void st_remote_f32(uint32_t cluster_addr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
-}
-
 // Sum of v over the column: over the warp (ONE), over the block, and over the cluster's blocks
 // where a column has several (each warp's sum goes to every block's buffer;
-// all add them in the same order).  buf: 8 * 32 floats, used once.
+// all add them in the same order).  buf: 8 * 32 floats, used once.  `started`:
+// the cluster's blocks are known to run.  Another block's shared memory may
+// not be touched before that, so every thread has arrived at the cluster's
+// barrier when it began, and waits for the others here, behind its loads.
 template <bool ONE>
-__device__ __forceinline__ float column_sum(float v, float* buf, int csize, int rank) {
+__device__ __forceinline__ float column_sum(float v, float* buf, int csize, int rank, bool& started) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     if (ONE) return v;
@@ -29,12 +28,10 @@ __device__ __forceinline__ float column_sum(float v, float* buf, int csize, int 
         if (lane == 0) buf[warp] = v;
         __syncthreads();
     } else {
-        if (lane < csize) {
-            uint32_t to;
-            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_u32(buf + rank * nw + warp)), "r"(lane));
-            st_remote_f32(to, v);
-        }
-        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+        if (!started) cluster_wait();
+        started = true;
+        if (lane < csize) st_cluster_f32(map_rank(smem_u32(buf + rank * nw + warp), lane), v);
+        cluster_sync();
     }
     float s = 0.f;
     for (int i = lane; i < csize * nw; i += 32) s += buf[i];
@@ -53,6 +50,8 @@ __device__ __forceinline__ float column_sum(float v, float* buf, int csize, int 
 template <bool VEC, int VPT, bool ONE>
 __global__ void __launch_bounds__(ONE ? 32 * kShortColumns : 1024) residual_kernel(ResidualArgs a) {
     __shared__ float buf[2][8 * 32];
+    bool started = ONE || a.csize == 1;
+    if (!started) cluster_arrive();
     pdl_wait();
     pdl_launch_dependents();
     const kq_residual& r = a.r;
@@ -118,7 +117,7 @@ __global__ void __launch_bounds__(ONE ? 32 * kShortColumns : 1024) residual_kern
             float sq = 0.f;
 #pragma unroll
             for (int i = 0; i < A * W; ++i) sq = fmaf(s[i], s[i], sq);
-            const float m = column_sum<ONE>(sq, buf[0], a.csize, rank) / static_cast<float>(a.N) + r.eps;
+            const float m = column_sum<ONE>(sq, buf[0], a.csize, rank, started) / static_cast<float>(a.N) + r.eps;
             k *= rsqrtf(m);
 #pragma unroll
             for (int i = 0; i < A * W; ++i) s[i] *= tmp[i];
@@ -139,11 +138,12 @@ __global__ void __launch_bounds__(ONE ? 32 * kShortColumns : 1024) residual_kern
         float sq = 0.f;
 #pragma unroll
         for (int i = 0; i < A * W; ++i) sq = fmaf(o[i], o[i], sq);  // (past the part's end: zeros)
-        const float k = rsqrtf(column_sum<ONE>(sq, buf[1], a.csize, rank) / static_cast<float>(a.N) + r.eps);
+        const float k = rsqrtf(column_sum<ONE>(sq, buf[1], a.csize, rank, started) / static_cast<float>(a.N) + r.eps);
 #pragma unroll
         for (int i = 0; i < A * W; ++i) o[i] *= k * tmp[i];
         store(r.h + t * r.ldh, o);
     }
+    if (!started) cluster_wait();  // (no norm)
 }
 
 template <bool VEC>
