@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1) attn_kernel(const __grid_c
     constexpr int RINGW = QS ? kRingShared : kRingAlone; // the ring per warp
     constexpr int NU = RINGW * TILES / UNIT;              // units of a stream's ring
     constexpr float PS = BF16 ? 0.f : 14.f;               // weights up to 2^14 keep the small ones normal in fp16
-    constexpr int TGT = BF16 ? 0 : 14;                    // a query row's largest value in [2^TGT, 2^(TGT+1))
+    constexpr int TGT = BF16 ? 0 : 14;                    // a query row's largest value in [2^TGT, 2^(TGT+1)), at the top of bf16 [2, 4)
     constexpr int PF = kPart<D, TR>;
 
     extern __shared__ __align__(1024) uint8_t ring_smem[];
@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1) attn_kernel(const __grid_c
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                     // a power of two per row takes the queries' size out of the terms
                     int e = (__float_as_int(mx) >> 23) - 127;
-                    e = mx > 0.f && mx < INFINITY ? min(max(e, -100), 127) : TGT;
+                    e = mx > 0.f && mx < INFINITY ? min(max(e, -100), TGT + 126) : TGT;  // (up is 2^-126 at least)
                     const float up = __int_as_float((TGT - e + 127) << 23);
                     dn[w] = __int_as_float((e - TGT + 127) << 23);
 #pragma unroll

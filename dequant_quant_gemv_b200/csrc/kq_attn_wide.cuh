@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
                     mx = fmaxf(fmaxf(mx, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(x.z), fabsf(x.w)));
                 }
                 int e = (__float_as_int(mx) >> 23) - 127;
-                e = mx > 0.f && mx < INFINITY ? min(max(e, -100), 127) : TGT;
+                e = mx > 0.f && mx < INFINITY ? min(max(e, -100), TGT + 126) : TGT;  // (up is 2^-126 at least)
                 const float up = __int_as_float((TGT - e + 127) << 23);
                 dn = __int_as_float((e - TGT + 127) << 23);
 #pragma unroll 1
