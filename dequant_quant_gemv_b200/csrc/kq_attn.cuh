@@ -38,7 +38,7 @@
 
 namespace kq {
 
-// A partial result: rows x D sums, then the rows' maxima, then their sums of
+// A partial result: rows x D sums, then the rows' bounds (bound_of), then their sums of
 // weights.  Slots per (block, tile): its first pair, begun in an earlier block;
 // its last, continued in a later one; and one per stream for a pair that
 // ends inside the stream after beginning before it.
@@ -62,6 +62,16 @@ __device__ __forceinline__ void ldm4t(uint32_t (&r)[4], uint32_t a) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(a)
                  : "memory");
+}
+
+// What is taken off a row's scores (in powers of two) of which `top` is the
+// largest: top rounded up to a whole number, any bound serves and this one's
+// factors are exact; less 14 against an f16 cache, as weights up to 2^14 keep
+// the small ones normal in fp16.  The difference is rounded up, so that no
+// weight is above 2^14 where the scores are so large that it is not exact.
+template <bool BF16>
+__device__ __forceinline__ float bound_of(float top) {
+    return BF16 ? ceilf(top) : __fsub_ru(ceilf(top), 14.f);
 }
 
 template <bool BF16>
@@ -309,7 +319,6 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1) attn_kernel(const __grid_c
     constexpr int S = kAttnWarps / TILES;                 // streams of the block
     constexpr int RINGW = QS ? kRingShared : kRingAlone; // the ring per warp
     constexpr int NU = RINGW * TILES / UNIT;              // units of a stream's ring
-    constexpr float PS = BF16 ? 0.f : 14.f;               // weights up to 2^14 keep the small ones normal in fp16
     constexpr int TGT = BF16 ? 0 : 14;                    // a query row's largest value in [2^TGT, 2^(TGT+1)), at the top of bf16 [2, 4)
     constexpr int PF = kPart<D, TR>;
 
@@ -634,9 +643,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1) attn_kernel(const __grid_c
                             if (key < row_lo[w] || key >= row_hi[w] || (bad_now >> (i >> 2) & 1)) s[w][i] = -INFINITY;
                         }
                 }
-                // ---- running maximum, rounded up to a whole power of two (any bound
-                // serves, and this one's factors are exact); the sums so far
-                // shrink where it grows
+                // ---- running bound of the scores; the sums so far shrink where it
+                // grows
 #pragma unroll
                 for (int w = 0; w < RW; ++w) {
                     float v = s[w][0];
@@ -644,14 +652,13 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1) attn_kernel(const __grid_c
                     for (int i = 1; i < 8; ++i) v = fmaxf(v, s[w][i]);
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-                    const float mn = fmaxf(m[w], ceilf(v * dn[w]));
+                    const float mn = fmaxf(m[w], bound_of<BF16>(v * dn[w]));
                     f[w] = ex2(m[w] - mn);
                     m[w] = mn;
-                    const float shift = PS - mn;
                     float sum = 0.f;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        s[w][i] = ex2(fmaf(s[w][i], dn[w], shift));
+                        s[w][i] = ex2(fmaf(s[w][i], dn[w], -mn));
                         sum += s[w][i];
                     }
                     l[w] = fmaf(l[w], f[w], sum);

@@ -115,7 +115,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
     constexpr uint32_t kColP = OVER ? kColS : kColS + 2 * CK, kColQ = kColP + 2 * TERMS * PT;
     static_assert(kBuf >= CK && kColQ + TERMS * QT <= kCols, "tensor memory");
     constexpr int STG = kWideStages<D>;
-    constexpr float PS = BF16 ? 0.f : 14.f;
     constexpr int TGT = BF16 ? 0 : 14;
     constexpr uint32_t TYPE = BF16 ? 1u : 0u;
     constexpr uint32_t IDESC = 1u << 4 | TYPE << 7 | TYPE << 10 | (128u >> 4) << 24;
@@ -497,15 +496,14 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
                     float v0 = s[0], v1 = s[1];
 #pragma unroll
                     for (int i = 2; i < CK; i += 2) v0 = fmaxf(v0, s[i]), v1 = fmaxf(v1, s[i + 1]);
-                    const float mn = fmaxf(m, ceilf(fmaxf(v0, v1) * dn));
+                    const float mn = fmaxf(m, bound_of<BF16>(fmaxf(v0, v1) * dn));
                     const float f = ex2(m - mn);
                     m = mn;
                     fs[n & 3][row] = f;
-                    const float shift = PS - mn;
                     float sum[2] = {0.f, 0.f};
 #pragma unroll
                     for (int i = 0; i < CK; ++i) {
-                        s[i] = ex2(fmaf(s[i], dn, shift));
+                        s[i] = ex2(fmaf(s[i], dn, -mn));
                         sum[i & 1] += s[i];
                     }
                     l = fmaf(l, f, sum[0] + sum[1]);

@@ -54,3 +54,35 @@ def test_queries_of_the_largest_binade(kv, n_q, D, size):
         out, V = call(kv, D, n_q, n, keys, sign * size)
         check(out, V, V[20] if sign > 0 else np.delete(V, 20, 0).mean(0))
 
+
+LARGE = [2.0 ** 24 - 3, 2.0 ** 25 + 4, 2.0 ** 25 + 12, 2.0 ** 26 + 8, 1e8, 2e8, 2.0 ** 28 + 32, 3e9]
+
+
+@pytest.mark.parametrize("kv", ["f16", "bf16"])
+@pytest.mark.parametrize("n_q,D", [(1, 64), (9, 64), (24, 128), (100, 64)])
+@pytest.mark.parametrize("size", LARGE)
+def test_scores_whose_step_is_large(kv, n_q, D, size):
+    """Equal scores weigh the same whatever their size; of unequal ones the largest has all."""
+    n = 90
+    out, V = call(kv, D, n_q, n, np.ones(n), size)
+    check(out, V, V.mean(0))
+    out, V = call(kv, D, n_q, n, np.ones(n), -size)
+    check(out, V, V.mean(0))
+    keys = np.full(n, 0.5)
+    keys[61] = 1.0
+    out, V = call(kv, D, n_q, n, keys, size)
+    check(out, V, V[61])
+    out, V = call(kv, D, n_q, n, keys, -size)
+    check(out, V, np.delete(V, 61, 0).mean(0))
+
+
+@pytest.mark.parametrize("kv", ["f16", "bf16"])
+@pytest.mark.parametrize("n_q", [1, 100])
+@pytest.mark.parametrize("size", [2.0 ** 25 + 4, 1e8, 2e8])
+def test_large_scores_over_many_blocks(kv, n_q, size):
+    """Parts with maxima of every size are joined."""
+    n = 5000
+    keys = np.zeros(n)
+    keys[3000], keys[3100] = 1.0, 1.0
+    out, V = call(kv, 64, n_q, n, keys, size)
+    check(out, V, (V[3000] + V[3100]) / 2)
