@@ -64,6 +64,10 @@ __device__ __forceinline__ void ldm4t(uint32_t (&r)[4], uint32_t a) {
                  : "memory");
 }
 
+// The bound of a row that has seen no key: the lowest finite value, so that it
+// is above no score.
+constexpr float kNoBound = -3.402823466e38f;
+
 // What is taken off a row's scores (in powers of two) of which `top` is the
 // largest: top rounded up to a whole number, any bound serves and this one's
 // factors are exact; less 14 against an f16 cache, as weights up to 2^14 keep
@@ -562,7 +566,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1) attn_kernel(const __grid_c
                             }
                         }
                     }
-                    m[w] = -3.0e38f;
+                    m[w] = kNoBound;
                     l[w] = 0.f;
                 }
                 if constexpr (QS) {
@@ -868,13 +872,13 @@ __global__ void __launch_bounds__(32 * kAttnWarps, 1) attn_kernel(const __grid_c
         float pm[2 * S], top[2 * S], pl[2 * S];
 #pragma unroll
         for (int q = 0; q < 2 * S; ++q) {
-            pm[q] = -3.0e38f, pl[q] = 0.f;
+            pm[q] = kNoBound, pl[q] = 0.f;
             if (has(q)) {
                 pm[q] = part_of(q, tl)[TR * D + row];
                 pl[q] = part_of(q, tl)[TR * D + TR + row];
             }
         }
-        float M = -3.0e38f, L = 0.f;
+        float M = kNoBound, L = 0.f;
 #pragma unroll
         for (int q = 0; q < 2 * S; ++q)
             if (has(q)) top[q] = M = begins(q) ? pm[q] : fmaxf(M, pm[q]);
@@ -1000,7 +1004,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i)
             if (i < n) v[i] = load_row<E>(part_of(i) + row * D + lane * E);
-        float M = -3.0e38f, L = 0.f;
+        float M = kNoBound, L = 0.f;
 #pragma unroll 1
         for (int i = lane; i < n; i += 32) {
             const float* p = part_of(i) + TR * D + row;

@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
             const bool live = 32 * warp < rows, mine = row < rows;
             const int tok = mine ? column_of(a, row) : at.q.n - 1;  // (a lane without a row keeps to the last one's keys)
             const int row_hi = at.q.len - (at.q.n - 1 - tok), row_lo = window_start(a, row_hi);
-            float m = -3.0e38f, l = 0.f, dn = 1.f;
+            float m = kNoBound, l = 0.f, dn = 1.f;
             if (live) {
                 // the queries' terms
                 asm volatile("cp.async.wait_group 0;" ::: "memory");

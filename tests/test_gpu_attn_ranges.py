@@ -86,3 +86,13 @@ def test_large_scores_over_many_blocks(kv, n_q, size):
     keys[3000], keys[3100] = 1.0, 1.0
     out, V = call(kv, 64, n_q, n, keys, size)
     check(out, V, (V[3000] + V[3100]) / 2)
+
+
+@pytest.mark.parametrize("kv", ["f16", "bf16"])
+@pytest.mark.parametrize("n_q,D", [(1, 64), (9, 64), (24, 128), (100, 64)])
+@pytest.mark.parametrize("n", [50, 2000])
+def test_scores_at_the_end_of_the_range(kv, n_q, D, n):
+    """Finite scores between -3e38 and the lowest fp32 value are scores, too."""
+    for size in (-2.9e38, -3.05e38, -3.3e38, 3.3e38):
+        out, V = call(kv, D, n_q, n, np.ones(n), size)
+        check(out, V, V.mean(0))
