@@ -65,7 +65,8 @@ int kq_kv_attn(int R, int64_t T, int max_q, int n_q, const float* q, int64_t ldq
         return layer_fail(KQ_ERR_UNSUPPORTED, "%d columns of %d query heads per key-value head: more than 128 rows",
                           max_q, n_q / n_kv);
     if (R > 8192 || T > INT32_MAX) return layer_fail(KQ_ERR_UNSUPPORTED, "R=%d T=%lld", R, (long long)T);
-    if (!(scale - scale == 0.f)) return layer_fail(KQ_ERR_INVALID_ARG, "scale is not finite");
+    const float scale2 = scale * 1.44269504088896340736f;  // the softmax is taken in powers of two
+    if (!(scale2 - scale2 == 0.f)) return layer_fail(KQ_ERR_INVALID_ARG, "scale=%g is not finite times log2(e)", scale);
     if (!q_start && T != R) return layer_fail(KQ_ERR_INVALID_ARG, "T=%lld without q_start is not R=%d", (long long)T, R);
     if (R == 0 || T == 0) return KQ_OK;
     if (static_cast<int64_t>(R) * max_pages > (int64_t(1) << 35) / cache->page_size)
@@ -99,7 +100,7 @@ int kq_kv_attn(int R, int64_t T, int max_q, int n_q, const float* q, int64_t ldq
     a.vec = aligned_to(q, 8) && aligned_to(out, 8) && ldq % 2 == 0 && ldo % 2 == 0;
     a.T = T, a.ldq = ldq, a.ldo = ldo, a.table_ld = table_ld, a.page_stride = cache->page_stride;
     a.n_pages = cache->n_pages;
-    a.scale = scale * 1.44269504088896340736f;
+    a.scale = scale2;
     a.q = q, a.k = cache->k, a.v = cache->v, a.lens = lens, a.q_start = q_start, a.table = table;
     a.out = out, a.status = status;
     a.head = static_cast<int4*>(workspace);

@@ -592,6 +592,10 @@ KQ_API int kq_kv_append(int64_t T, const float* qkv, int64_t ld, int n_q, const 
  * of two per row) and exp(s_i) enter the tensor cores as two fp16 terms (22
  * bits) against an f16 cache, as three bf16 terms (24 bits) against a bf16
  * cache, so an output differs from the exact one by a few fp32 roundings.
+ * In fp32, scale * log2(e) must be finite (KQ_ERR_INVALID_ARG), and so must
+ * q * scale * log2(e) and every s_i * log2(e); beyond that a column's result
+ * is NaN or zeros.  The same holds for a key of a bf16 cache whose |k_d| add up
+ * to 2^126 or more (the products are made of queries scaled to at most 4).
  * R <= 8192, R * max_pages * page_size <= 2^35, n_q a multiple of n_kv with
  * max_q * n_q/n_kv <= 128 (KQ_ERR_UNSUPPORTED beyond).
  */
