@@ -388,6 +388,13 @@ def _mat(dev: int, t: torch.Tensor, name: str, dtype, rows: int, cols: int) -> t
     return t.data_ptr(), t.stride(0) if rows > 1 else cols
 
 
+def _int(v: int, name: str) -> int:
+    """A whole number that fits the C ABI's int (ctypes would cut it)."""
+    if not -2 ** 31 <= v < 2 ** 31:
+        raise ValueError(f"{name}={v} does not fit in 32 bits")
+    return v
+
+
 def _index(t: torch.Tensor, what: str) -> int:
     dev = t.get_device()
     if dev < 0:
@@ -473,8 +480,8 @@ def kv_plan(lens: torch.Tensor, add: torch.Tensor, table: torch.Tensor, free_pag
     width, n_stack, p = table.shape[-1], free_pages.numel(), plan._ptr
     tab, ld = _mat(dev, table, "table", i32, R, width)
     _layer_call(_layer_lib().kq_kv_plan, "kq_kv_plan", dev, stream, R, _vec(dev, lens, "lens", i32, R),
-                _vec(dev, add, "add", i32, R), page_size, tab, ld, width, _vec(dev, free_pages, "free_pages", i32, n_stack),
-                n_stack, _vec(dev, n_free, "n_free", i32, 1), plan._T, p[0], p[1], p[2], p[3], p[4],
+                _vec(dev, add, "add", i32, R), _int(page_size, "page_size"), tab, ld, width,
+                _vec(dev, free_pages, "free_pages", i32, n_stack), n_stack, _vec(dev, n_free, "n_free", i32, 1), plan._T, p[0], p[1], p[2], p[3], p[4],
                 _opt(dev, status, "status", i32, 1))
     return plan
 
@@ -519,7 +526,8 @@ def kv_append(qkv: torch.Tensor, n_q: int, cache: KVCache, slots: torch.Tensor, 
 def kv_attn_workspace_bytes(R: int, max_q: int, n_q: int, cache: KVCache) -> int:
     """Bytes of kv_attn's workspace (kq_kv_attn_workspace_bytes), on the cache's device."""
     with torch.cuda.device(cache._dev):
-        return int(_layer_lib().kq_kv_attn_workspace_bytes(R, max_q, n_q, cache._ref))
+        return int(_layer_lib().kq_kv_attn_workspace_bytes(_int(R, "R"), _int(max_q, "max_q"), _int(n_q, "n_q"),
+                                                            cache._ref))
 
 
 def kv_attn(q: torch.Tensor, cache: KVCache, lens: torch.Tensor, table: torch.Tensor,
@@ -541,7 +549,7 @@ def kv_attn(q: torch.Tensor, cache: KVCache, lens: torch.Tensor, table: torch.Te
             return out
     dev, f32, i32, D = cache._dev, torch.float32, torch.int32, cache.head_dim
     T, cols = q.shape
-    n_q, R, width = cols // D, lens.numel(), table.shape[-1]
+    n_q, R, width, max_q, window = cols // D, lens.numel(), table.shape[-1], _int(max_q, "max_q"), _int(window, "window")
     if n_q * D != cols:
         raise ValueError(f"q must have head_dim = {D} columns per head, got {cols}")
     x, ldq = _mat(dev, q, "q", f32, T, cols)
