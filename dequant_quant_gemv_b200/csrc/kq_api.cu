@@ -479,8 +479,17 @@ static int plan_for(int fmt, int k, bool mma, GemvArgs& a, LaunchPlan& p) {
 
 // kq_inject("hold@S"): the next single-column launch withholds stage S of
 // CTA 0 and gives its bounded waits 1 ms (one-shot; 0 = none).
-static std::atomic<int> g_inject_hold{0};
+// "hold_attn@N": the same for chunk N of the first block of the next
+// attention call of many rows.
+static std::atomic<int> g_inject_hold{0}, g_inject_attn{0};
 constexpr unsigned long long kInjectWaitNs = 1000000ull;
+
+int take_attn_hold(unsigned long long* wait_ns) {
+    if (g_inject_attn.load(std::memory_order_relaxed) == 0) return 0;
+    const int hold = g_inject_attn.exchange(0);
+    if (hold) *wait_ns = kInjectWaitNs;
+    return hold;
+}
 
 static int run(GemvArgs& a, int fmt, int k, bool mma, cudaStream_t stream) {
     a.ncol_real = k;
@@ -620,13 +629,15 @@ int kq_inject(const char* spec) {
     g_last_error[0] = 0;
     if (!spec || !spec[0]) {
         g_inject_hold.store(0);
+        g_inject_attn.store(0);
         return KQ_OK;
     }
-    if (strncmp(spec, "hold@", 5) == 0) {
+    const bool attn = strncmp(spec, "hold_attn@", 10) == 0;
+    if (attn || strncmp(spec, "hold@", 5) == 0) {
         char* end = nullptr;
-        const long v = strtol(spec + 5, &end, 10);
+        const long v = strtol(spec + (attn ? 10 : 5), &end, 10);
         if (end && *end == 0 && v >= 1 && v <= 1000000) {
-            g_inject_hold.store(static_cast<int>(v));
+            (attn ? g_inject_attn : g_inject_hold).store(static_cast<int>(v));
             return KQ_OK;
         }
     }

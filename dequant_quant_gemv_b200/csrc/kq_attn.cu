@@ -1,5 +1,6 @@
 // kq_attn.cu — the entry point of attention over the paged cache.
 #include "kq_attn.h"
+#include "kq_device.cuh"
 
 namespace kq {
 
@@ -106,7 +107,11 @@ int kq_kv_attn(int R, int64_t T, int max_q, int n_q, const float* q, int64_t ldq
     a.head = static_cast<int4*>(workspace);
     a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + head_bytes(sms));
     const bool many = wide(rows, static_cast<int64_t>(max_pages) * cache->page_size, window);
-    if (many) a.tiles = (rows + 15) / 16;
+    a.wait_ns = kWaitNs;
+    if (many) {
+        a.tiles = (rows + 15) / 16;
+        a.test_hold = take_attn_hold(&a.wait_ns);
+    }
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool b = cache->type == KQ_KV_BF16;
     if (many)

@@ -31,6 +31,8 @@ struct AttnArgs {
                                    // kv head}, {the block that it ends in}
     float* part;                   // partial results (see kPart)
     int* fault;                    // device fault word (a wait that ran out)
+    unsigned long long wait_ns;    // limit of a wait
+    int test_hold;                 // test hook: the first block's keys of this chunk (from 1) are not handed on; 0: none
 };
 
 // More rows per pair than kTileRows always take the kernel for many rows

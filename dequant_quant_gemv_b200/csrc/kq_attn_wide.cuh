@@ -13,7 +13,8 @@
 // Roles: four warps of softmax; four that sum the weighted values; one that
 // issues the products; one that copies keys and one that copies values, three
 // chunks on their way.  They hand each other chunks through barriers in shared
-// memory, every wait bounded.  The products of a chunk wait on one barrier, at
+// memory, every wait bounded: one that runs out sets the fault word and ends the
+// block's roles, and what is in flight lands before the block exits.  The products of a chunk wait on one barrier, at
 // which the softmax (4 warps), the sums of the chunk before (4) and the values (1)
 // arrive.  While the softmax of a chunk runs, the weighted values of the chunk
 // before are made, and the scores of the next.
@@ -129,7 +130,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
     // n & 1; a barrier of a stage or buffer completes once per use of it, the
     // others once per chunk or pair
     __shared__ uint64_t full_k[STG], full_v[STG], empty_k[STG], empty_v[STG];
-    __shared__ uint64_t s_ready[2], q_ready, p_ready[4], y_ready, l_ready[4];
+    __shared__ uint64_t s_ready[2], q_ready, p_ready[4], y_ready, l_ready[4], drained;
     __shared__ uint32_t tmem_addr;
     __shared__ int gave_up, marked;
     pdl_wait();
@@ -155,6 +156,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
         }
         mbar_init(&q_ready, 4);
         mbar_init(&y_ready, 1);
+        mbar_init(&drained, 1);
         fence_barrier_init();
         gave_up = marked = 0;
     }
@@ -187,7 +189,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
             if (there || (i & 63)) continue;
             const unsigned long long t = globaltimer_ns();
             if (t0 == 0) t0 = t;
-            if (*const_cast<volatile int*>(&gave_up) || t - t0 > kWaitNs) break;
+            if (*const_cast<volatile int*>(&gave_up) || t - t0 > a.wait_ns) break;
         }
         const bool done = __all_sync(0xffffffffu, there);
         if (!done && lane == 0) {
@@ -271,6 +273,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
                     if (all(c + 2 < c_stop) && (good = keys_in(n + 2) && (!OVER || wait_for(&y_ready, n)))) scores(n + 2);
                 }
             } while (good && all(follow(at, c, c_stop)));
+            // nothing that was issued may run on when tensor and shared memory are
+            // given back (after a wait that ran out, in any warp, nobody else has
+            // waited for it)
+            if (elect_one()) commit(&drained);
+            __syncwarp();
+            mbar_wait_drain(&drained, 0);
         } else if ((warp == kAttnWarps + 1 || warp == kAttnWarps + 2) && some) {
             // ---- copies of keys, or of values: pages in batches of 8 chunks
             // (one per lane and 16 keys), as in attn_kernel
@@ -307,7 +315,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) attn_wide_kernel(const __grid
             const int lane_src = row0 * D + x * 8;
             uint32_t n = 0;
             bool good = true;
-            auto hand = [&](uint32_t m) { give(&full[m % STG], lv ? &p_ready[m & 3] : nullptr); };
+            auto hand = [&](uint32_t m) {
+                if (a.test_hold == static_cast<int>(m) + 1 && !lv && blockIdx.x == 0) return;
+                give(&full[m % STG], lv ? &p_ready[m & 3] : nullptr);
+            };
             for (; good && lc < le; ++n) {
                 if (n >= STG && !wait_for(&empty[n % STG], n / STG - 1)) {
                     good = false;

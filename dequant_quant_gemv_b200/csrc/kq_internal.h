@@ -134,6 +134,8 @@ cudaError_t ensure_smem_attr(const void* func, size_t bytes);
 // Read-only bandwidth probes (kq_read_probe): mode 0 loads, mode 1 bulk-copy ring.
 cudaError_t launch_probe(const void* src, size_t bytes, int mode, uint32_t* out, int sm_count, cudaStream_t s);
 cudaError_t read_and_clear_fault(int* out);
+// kq_inject("hold_attn@N"): N once after it (and the shortened limit of the waits), else 0.
+int take_attn_hold(unsigned long long* wait_ns);
 // The current device's number of SMs (looked up once per device).
 cudaError_t device_sms(int* out);
 // Records `msg` as the calling thread's kq_last_error() text; returns status.

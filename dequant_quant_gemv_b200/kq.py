@@ -280,7 +280,8 @@ def read_probe(buf: torch.Tensor, mode: int, out: torch.Tensor, stream=None) -> 
 
 def inject(spec: str | None) -> None:
     """kq_inject: test hook ("hold@S" withholds one weight stage of the next
-    single-column launch so that its bounded wait runs out)."""
+    single-column launch, "hold_attn@N" one chunk of keys of the next attention
+    call of many rows, so that a bounded wait runs out)."""
     L = lib()
     L.kq_inject.restype = ctypes.c_int
     L.kq_inject.argtypes = [ctypes.c_char_p]
@@ -481,7 +482,8 @@ def kv_plan(lens: torch.Tensor, add: torch.Tensor, table: torch.Tensor, free_pag
     tab, ld = _mat(dev, table, "table", i32, R, width)
     _layer_call(_layer_lib().kq_kv_plan, "kq_kv_plan", dev, stream, R, _vec(dev, lens, "lens", i32, R),
                 _vec(dev, add, "add", i32, R), _int(page_size, "page_size"), tab, ld, width,
-                _vec(dev, free_pages, "free_pages", i32, n_stack), n_stack, _vec(dev, n_free, "n_free", i32, 1), plan._T, p[0], p[1], p[2], p[3], p[4],
+                _vec(dev, free_pages, "free_pages", i32, n_stack), n_stack, _vec(dev, n_free, "n_free", i32, 1), plan._T,
+                p[0], p[1], p[2], p[3], p[4],
                 _opt(dev, status, "status", i32, 1))
     return plan
 

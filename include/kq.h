@@ -147,7 +147,10 @@ KQ_API int kq_device_fault(int* out);
  * the consumers waiting for that stage then time out, the CTA stops, lets
  * the copies it issued land, and the launch ends with the fault word set to
  * KQ_ERR_TIMEOUT (read it with kq_device_fault); that CTA's outputs are
- * undefined.  One-shot; NULL or "" cancels.  No trap, no hang: the context
+ * undefined.  spec "hold_attn@N" (N >= 1): the same for the next kq_kv_attn
+ * call that takes the kernel for many rows (more than 64 query rows per
+ * key-value head, say): its first block does not hand on the keys of its N-th
+ * chunk of 64, if it has as many.  One-shot; NULL or "" cancels.  No trap, no hang: the context
  * stays usable.  Process-wide; KQ_ERR_INVALID_ARG for another spec. */
 KQ_API int kq_inject(const char* spec);
 
@@ -588,6 +591,9 @@ KQ_API int kq_kv_append(int64_t T, const float* qkv, int64_t ld, int n_q, const 
  *   Device checks (set *status): a request whose q_start leaves [0, T] or has
  *   n_r outside 0..max_q is left out; lens outside 0..max_pages*page_size (and
  *   2^31 - 1024) is clamped to it; keys of a page number outside [0, n_pages) are not seen.
+ * With many rows per key-value head the kernel's warps wait for one another,
+ * 2 s at most; a wait that runs out sets the device fault word
+ * (kq_device_fault) to KQ_ERR_TIMEOUT, and the call's outputs are undefined.
  * The softmax's maximum and sum and the outputs are fp32.  q (after a power
  * of two per row) and exp(s_i) enter the tensor cores as two fp16 terms (22
  * bits) against an f16 cache, as three bf16 terms (24 bits) against a bf16
