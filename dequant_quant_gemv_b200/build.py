@@ -40,6 +40,14 @@ FLAGS = [*ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcomp
          "-I", os.path.join(ROOT, "include")]
 
 
+def calls_key() -> str:
+    """What _calls.so is built against: another torch, C++ ABI or Python needs another one."""
+    import sysconfig
+
+    import torch
+    return f"{torch.__version__} {int(torch._C._GLIBCXX_USE_CXX11_ABI)} {sysconfig.get_config_var('SOABI')}"
+
+
 def _calls_command(out: str) -> list[str]:
     import sysconfig
 
@@ -49,15 +57,23 @@ def _calls_command(out: str) -> list[str]:
     inc = [*include_paths(), sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     return ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
-            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DKQ_CALLS_KEY="{calls_key()}"',
             *[x for d in inc for x in ("-isystem", d)], "-o", out, CALLS_SRC,
             f"-L{lib}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
+def _calls_current() -> bool:
+    """Whether _calls.so is newer than its sources and built against this torch and Python."""
+    if not os.path.exists(CALLS):
+        return False
+    newest = max(os.path.getmtime(f) for f in (CALLS_SRC, os.path.join(ROOT, "include", "kq.h"), os.path.abspath(__file__)))
+    with open(CALLS, "rb") as f:
+        return os.path.getmtime(CALLS) >= newest and calls_key().encode() + b"\0" in f.read()
+
+
 def build_calls(force: bool = False):
     """Start building _calls.so where it is out of date: (process, temporary file), or None."""
-    newest = max(os.path.getmtime(f) for f in (CALLS_SRC, os.path.join(ROOT, "include", "kq.h"), os.path.abspath(__file__)))
-    if not force and os.path.exists(CALLS) and os.path.getmtime(CALLS) >= newest:
+    if not force and _calls_current():
         return None
     tmp = CALLS + f".tmp{os.getpid()}"
     return subprocess.Popen(_calls_command(tmp), stdout=subprocess.PIPE, stderr=subprocess.STDOUT), tmp

@@ -271,4 +271,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nul
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__calls(void) { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__calls(void) {
+    PyObject* m = PyModule_Create(&module);
+    // what this file was built against; the binding takes it for nothing else
+    if (m && PyModule_AddStringConstant(m, "key", KQ_CALLS_KEY) < 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}

@@ -342,6 +342,9 @@ def _layer_lib() -> ctypes.CDLL:
             from . import _calls
         except ImportError as e:
             raise ImportError("_calls.so not built; run python -m dequant_quant_gemv_b200.build") from e
+        from .build import calls_key
+        if getattr(_calls, "key", None) != calls_key():
+            raise ImportError("_calls.so is built against another torch or Python; run python -m dequant_quant_gemv_b200.build")
         _calls.use(*[ctypes.cast(f, ctypes.c_void_p).value
                      for f in (L.kq_kv_plan, L.kq_kv_append, L.kq_kv_attn, L.kq_residual_norm)])
         _layer, _fast = L, _calls
