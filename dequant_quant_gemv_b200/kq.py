@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 
 import numpy as np
 
@@ -322,6 +323,26 @@ _layer = None
 _fast = None   # the compiled fast path (csrc/kq_calls.cpp)
 
 
+class _NoFastPath:
+    """Takes no call, so that each goes through ctypes to the same C ABI."""
+    kv_plan = kv_append = kv_attn = residual_norm = staticmethod(lambda *a: None)
+
+
+def _fast_path(L: ctypes.CDLL):
+    from .build import calls_key
+    try:
+        from . import _calls
+        if getattr(_calls, "key", None) != calls_key():
+            raise ImportError("built against another torch or Python")
+    except ImportError as e:
+        warnings.warn(f"_calls.so cannot be used ({e}): the layer operators' calls take about 5 us longer on the host; "
+                      "run python -m dequant_quant_gemv_b200.build", RuntimeWarning, stacklevel=4)
+        return _NoFastPath
+    _calls.use(*[ctypes.cast(f, ctypes.c_void_p).value
+                 for f in (L.kq_kv_plan, L.kq_kv_append, L.kq_kv_attn, L.kq_residual_norm)])
+    return _calls
+
+
 def _layer_lib() -> ctypes.CDLL:
     global _layer, _fast
     if _layer is None:
@@ -338,16 +359,8 @@ def _layer_lib() -> ctypes.CDLL:
                                  vp, sz, vp, vp]
         L.kq_residual_norm.restype = i32
         L.kq_residual_norm.argtypes = [vp, i64, i64, vp]
-        try:
-            from . import _calls
-        except ImportError as e:
-            raise ImportError("_calls.so not built; run python -m dequant_quant_gemv_b200.build") from e
-        from .build import calls_key
-        if getattr(_calls, "key", None) != calls_key():
-            raise ImportError("_calls.so is built against another torch or Python; run python -m dequant_quant_gemv_b200.build")
-        _calls.use(*[ctypes.cast(f, ctypes.c_void_p).value
-                     for f in (L.kq_kv_plan, L.kq_kv_append, L.kq_kv_attn, L.kq_residual_norm)])
-        _layer, _fast = L, _calls
+        _fast = _fast_path(L)
+        _layer = L
     return _layer
 
 
