@@ -86,6 +86,8 @@ def finish_calls(started) -> None:
     out, _ = p.communicate()
     if p.returncode:
         sys.stdout.write(out.decode(errors="replace"))
+        if os.path.exists(tmp):
+            os.remove(tmp)
         raise RuntimeError("g++ failed for kq_calls.cpp")
     os.replace(tmp, CALLS)
 
@@ -93,9 +95,15 @@ def finish_calls(started) -> None:
 def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -> str:
     """Compile every csrc/*.cu to an object (in parallel), link libkq.so, and build _calls.so."""
     calls = build_calls(force)
-    if not force and up_to_date():
+    try:
+        if force or not up_to_date():
+            _build_lib(verbose)
+    finally:
         finish_calls(calls)
-        return LIB
+    return LIB
+
+
+def _build_lib(verbose: bool) -> None:
     objdir = os.path.join(PKG, "_build")
     os.makedirs(objdir, exist_ok=True)
     procs, objs = [], []
@@ -118,8 +126,6 @@ def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -
     tmp = LIB + f".tmp{os.getpid()}"
     subprocess.check_call([NVCC, *ARCH, "--shared", "-o", tmp, *objs])
     os.replace(tmp, LIB)
-    finish_calls(calls)
-    return LIB
 
 
 if __name__ == "__main__":

@@ -57,3 +57,26 @@ def test_the_operators_work_without_it(monkeypatch):
     x, g = torch.zeros(2, 64), torch.ones(64)
     with pytest.raises(ValueError):  # the checks in Python
         kq.residual_norm(x, x, pre_gamma=g, out=x.clone(), h=x.clone())
+
+
+def test_a_failed_kernel_leaves_no_child_behind(monkeypatch, tmp_path):
+    """_calls.so is compiled beside the kernels: it is waited for when one of them fails."""
+    child = Child()
+    tmp = tmp_path / "_calls.so.tmp"
+    tmp.write_bytes(b"made")
+    monkeypatch.setattr(build, "build_calls", lambda force=False: (child, str(tmp)))
+    monkeypatch.setattr(build, "CALLS", str(tmp_path / "_calls.so"))
+    monkeypatch.setattr(build, "sources", lambda: [str(tmp_path / "none.cu")])
+    with pytest.raises(RuntimeError, match="nvcc failed"):
+        build.build(force=True)
+    assert child.collected and not tmp.exists()
+
+
+def test_a_failed_one_leaves_no_temporary_file(monkeypatch, tmp_path):
+    child = Child()
+    child.returncode = 1
+    tmp = tmp_path / "_calls.so.tmp"
+    tmp.write_bytes(b"half of it")
+    with pytest.raises(RuntimeError, match="kq_calls.cpp"):
+        build.finish_calls((child, str(tmp)))
+    assert not tmp.exists()
