@@ -1,5 +1,6 @@
 """Build libkq.so (the CUDA kernels and the C ABI) in-tree for sm_100a, and
-_calls.so (the binding's fast path) against the installed torch.
+_calls.so (the binding's fast path) against the installed torch, where that
+has its headers and there is a g++.
 
     python -m dequant_quant_gemv_b200.build [--force]
 """
@@ -7,6 +8,7 @@ from __future__ import annotations
 
 import glob
 import os
+import shutil
 import subprocess
 import sys
 
@@ -48,14 +50,32 @@ def calls_key() -> str:
     return f"{torch.__version__} {int(torch._C._GLIBCXX_USE_CXX11_ABI)} {sysconfig.get_config_var('SOABI')}"
 
 
-def _calls_command(out: str) -> list[str]:
+def _calls_dirs() -> tuple[list[str], str]:
+    """Where _calls.so's headers and libraries are."""
     import sysconfig
 
     import torch
     from torch.utils.cpp_extension import include_paths
     cuda = os.path.dirname(os.path.dirname(NVCC))
-    inc = [*include_paths(), sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
-    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    return ([*include_paths(), sysconfig.get_paths()["include"], os.path.join(cuda, "include")],
+            os.path.join(os.path.dirname(torch.__file__), "lib"))
+
+
+def _calls_lack() -> str | None:
+    """What _calls.so needs and is not there."""
+    inc, lib = _calls_dirs()
+    for header in ("torch/csrc/autograd/python_variable.h", "c10/cuda/CUDAStream.h", "Python.h", "cuda_runtime_api.h"):
+        if not any(os.path.exists(os.path.join(d, header)) for d in inc):
+            return header
+    for so in ("libtorch_python.so", "libc10_cuda.so"):
+        if not os.path.exists(os.path.join(lib, so)):
+            return so
+    return None if shutil.which("g++") else "g++"
+
+
+def _calls_command(out: str) -> list[str]:
+    import torch
+    inc, lib = _calls_dirs()
     return ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DKQ_CALLS_KEY="{calls_key()}"',
             *[x for d in inc for x in ("-isystem", d)], "-o", out, CALLS_SRC,
@@ -74,6 +94,10 @@ def _calls_current() -> bool:
 def build_calls(force: bool = False):
     """Start building _calls.so where it is out of date: (process, temporary file), or None."""
     if not force and _calls_current():
+        return None
+    lack = _calls_lack()
+    if lack:  # (the binding calls through ctypes then; a compilation that fails is an error)
+        print(f"_calls.so is not built: no {lack}")
         return None
     tmp = CALLS + f".tmp{os.getpid()}"
     return subprocess.Popen(_calls_command(tmp), stdout=subprocess.PIPE, stderr=subprocess.STDOUT), tmp

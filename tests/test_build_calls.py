@@ -80,3 +80,19 @@ def test_a_failed_one_leaves_no_temporary_file(monkeypatch, tmp_path):
     with pytest.raises(RuntimeError, match="kq_calls.cpp"):
         build.finish_calls((child, str(tmp)))
     assert not tmp.exists()
+
+
+def test_without_torchs_headers_it_is_left_out(monkeypatch, tmp_path, capsys):
+    """The library needs neither torch's headers nor g++."""
+    import torch.utils.cpp_extension as ext
+    monkeypatch.setattr(build.subprocess, "Popen", Child)
+    monkeypatch.setattr(ext, "include_paths", lambda *a, **k: [str(tmp_path)])
+    assert build.build_calls(force=True) is None
+    assert "python_variable.h" in capsys.readouterr().out
+
+
+def test_without_a_compiler_it_is_left_out(monkeypatch, tmp_path, capsys):
+    monkeypatch.setattr(build.subprocess, "Popen", Child)
+    monkeypatch.setenv("PATH", str(tmp_path))
+    assert build.build_calls(force=True) is None
+    assert "g++" in capsys.readouterr().out
