@@ -171,8 +171,8 @@ int kq_residual_norm(const kq_residual* r, int64_t T, int64_t N, kq_stream_t str
     if (r->n_terms < 0) return layer_fail(KQ_ERR_INVALID_ARG, "n_terms=%d", r->n_terms);
     if (N > 131072 || r->n_terms > 256)
         return layer_fail(KQ_ERR_UNSUPPORTED, "N=%lld n_terms=%d", (long long)N, r->n_terms);
-    if (!r->out && !r->h) return layer_fail(KQ_ERR_INVALID_ARG, "neither out nor h");
     if (T == 0 || N == 0) return KQ_OK;
+    if (!r->out && !r->h) return layer_fail(KQ_ERR_INVALID_ARG, "neither out nor h");
     if (r->n_terms > 0 && (!good(r->y, 4) || r->ldy < 0 || r->ld_term < 0 || (r->n_terms > 1 && r->ld_term < N) ||
                            (T > 1 && r->ldy < N)))
         return layer_fail(KQ_ERR_INVALID_ARG, "y: NULL, misaligned, or strides below N");
