@@ -45,8 +45,9 @@ __device__ __forceinline__ float column_sum(float v, float* buf, int csize, int 
 // the blocks of a cluster, whose sums meet in shared memory.  Bound by the
 // bytes for many columns, by load latency and the two reductions for few.
 // 2048 columns of eight routed rows of 2048: 34 us, 5.9 TB/s, 90% of a copy; one
-// column of 4096: 2.3 us.  Short columns take a warp each (ONE): 60000
-// columns of 100 take 19 us, and took 62 with a block each.
+// column of 4096: 2.3 us, and no more than without the wait for the cluster's
+// start.  Short columns take a warp each (ONE): 60000 columns of 100 take 19 us,
+// and took 62 with a block each.
 template <bool VEC, int VPT, bool ONE>
 __global__ void __launch_bounds__(ONE ? 32 * kShortColumns : 1024) residual_kernel(ResidualArgs a) {
     __shared__ float buf[2][8 * 32];
