@@ -38,7 +38,10 @@ struct PlanArgs {
     int64_t* slots;
 };
 
-constexpr int kPlanThreads = 256, kPlanThreadsMany = 1024;  // the latter above 1024 requests
+// Threads of a block, the latter above kPlanMany requests.  With 256 / 1024 (us):
+// 8 requests 3.2 / 5.0, 1024 5.8 / 6.8, 1500 6.8 / 7.6, 2048 8.0 / 8.1, 4096
+// 14.8 / 10.2, 8192 25.8 / 14.8.
+constexpr int kPlanThreads = 256, kPlanThreadsMany = 1024, kPlanMany = 2048;
 
 // Largest i in [0, n) with v[i] <= x, for v[0] <= x and v ascending.
 __device__ __forceinline__ int last_not_above(const int* v, int n, int x) {
@@ -405,7 +408,7 @@ int kq_kv_plan(int R, const int32_t* lens, const int32_t* add, int page_size, in
     if (err != cudaSuccess) return layer_fail(KQ_ERR_CUDA, "device query: %s", cudaGetErrorString(err));
     PlanArgs a{R, log2_of(page_size), max_pages, free_cap, T, table_ld, lens, add, free_pages, n_free,
                table, new_lens, q_start, pos, n_left, status, slots};
-    const int threads = R > 1024 ? kPlanThreadsMany : kPlanThreads;
+    const int threads = R > kPlanMany ? kPlanThreadsMany : kPlanThreads;
     const int64_t want = (T + threads - 1) / threads;
     const int grid = static_cast<int>(want < 1 ? 1 : want > sms ? sms : want);
     const size_t smem = sizeof(int) * 2 * (static_cast<size_t>(R) + 1);
